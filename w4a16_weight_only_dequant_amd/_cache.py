@@ -12,11 +12,12 @@ import functools
 
 import torch
 
-from ._lib import W4A16_BF16, W4A16_F16, _check, _default_workspace, _lib, _sz, _workspaces
+from ._lib import W4A16_BF16, W4A16_F16, _check, _lib, _scratch, _sz, _workspaces
 
 _CODES = {torch.float16: W4A16_F16, torch.bfloat16: W4A16_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_capturing_here = torch.cuda.is_current_stream_capturing
 _append_call = _lib.w4a16_kv_append
 _attention_call = _lib.w4a16_attention
 
@@ -170,7 +171,8 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
     dim ** -0.5 by default. window and sinks: a token sees the last `window`
     keys (itself among them) and the first `sinks` of its sequence; 0: all.
     Returns the output, in `out` or a new tensor; lse float32 [tokens][heads],
-    where given, gets ln sum exp of each row's scores."""
+    where given, gets ln sum exp of each row's scores. workspace: a Workspace
+    instead of the stream's own (under capture, of memory of the graph)."""
     if stream is not None:
         return _on_stream(attention, stream, out is None, q, k_cache, v_cache, page_table, kv_lens, q_starts=q_starts,
                           max_q_len=max_q_len, max_kv_len=max_kv_len, scale=scale, window=window, sinks=sinks, out=out,
@@ -206,20 +208,19 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
         os = _out_rows("out", out, shape, dtype, dev)
     nbytes = attention_workspace_bytes(batch, heads, kvh, dim, max_q_len, max_kv_len, window, sinks)
     raw = _raw_stream(dev)
-    ws_ptr = None
+    buf = None   # held until the call is queued
     if nbytes:
-        ws = _workspaces.get((dev, raw)) if workspace is None else None
+        ws = _workspaces.get((dev, raw)) if workspace is None and not _capturing_here() else None
         if ws is not None and ws.buf is not None and ws.buf.numel() >= nbytes and ws._alloc_stream.cuda_stream == raw:
-            ws_ptr = ws.buf.data_ptr()   # (allocated on this stream: nothing to record)
+            buf = ws.buf   # (allocated on this stream: nothing to record)
         else:
-            strm = torch.cuda.current_stream(dev)
-            ws_ptr = (workspace or _default_workspace(k_cache.device, strm)).get(nbytes, strm).data_ptr()
+            buf = _scratch(workspace, k_cache.device, torch.cuda.current_stream(dev), nbytes)
     status = _attention_call(
         q.data_ptr(), qs, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, page_stride, page_table.data_ptr(),
         strides[0] if batch > 1 else columns, _index("kv_lens", kv_lens, torch.int32, (batch,), dev), starts,
         tokens, batch, heads, kvh, dim, max_q_len, max_kv_len, dim ** -0.5 if scale is None else scale, window, sinks,
-        out.data_ptr(), os, None if lse is None else _index("lse", lse, torch.float32, (tokens, heads), dev), ws_ptr,
-        nbytes, raw)
+        out.data_ptr(), os, None if lse is None else _index("lse", lse, torch.float32, (tokens, heads), dev),
+        None if buf is None else buf.data_ptr(), nbytes, raw)
     if status:
         _check("w4a16_attention", status)
     return out

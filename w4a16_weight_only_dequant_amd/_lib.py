@@ -250,6 +250,14 @@ def unpack(pw: PackedWeight, stream=None):
     return codes, s_out, z_out
 
 
+def _capturing(stream=None) -> bool:
+    """Whether `stream` (None: the current one) records a graph."""
+    if stream is None or stream == torch.cuda.current_stream():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
     """Device workspace handed to the compute calls.
 
@@ -260,17 +268,32 @@ class Workspace:
     A buffer used on a stream other than the one it was allocated on is
     recorded on that stream, so that the caching allocator does not hand its
     memory out again before the work queued there is done.
+
+    A graph keeps the address that its captured calls were given: a buffer
+    handed out under capture is never freed while the workspace lives, also
+    where a later call needs a larger one. Graphs captured with one workspace
+    must not replay at the same time.
     """
 
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda")
         self.buf = None
         self._alloc_stream = None
+        self._captured = False   # a graph holds self.buf's address
+        self._outgrown = []      # buffers that graphs still hold
 
     def get(self, nbytes: int, stream=None):
         if nbytes == 0:
             return None
+        buf = self._fit(nbytes, stream)
+        self._captured = self._captured or _capturing(stream)
+        return buf
+
+    def _fit(self, nbytes: int, stream):
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._outgrown.append(self.buf)
+                self._captured = False
             # the old buffer (if any) was recorded on every stream that used it
             self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
             self._alloc_stream = torch.cuda.current_stream(self.device)
@@ -294,6 +317,22 @@ def _default_workspace(device, stream) -> Workspace:
     return ws
 
 
+def _scratch(workspace, device, stream, nbytes: int):
+    """The buffer of one call (None: it needs none): from the caller's
+    workspace, or by default from the stream's own. Under capture the default
+    is memory of the graph itself: torch.cuda.graph's pool keeps it for as long
+    as the graph lives, and no other graph or eager call is given it. (A capture
+    begun otherwise, without such a pool, needs a Workspace of the caller's.)"""
+    if nbytes == 0:
+        return None
+    if workspace is not None:
+        return workspace.get(nbytes, stream)
+    if _capturing(stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _default_workspace(device, stream)._fit(nbytes, stream)
+
+
 def _output(out, M: int, N: int, x: torch.Tensor) -> torch.Tensor:
     """`out`, checked to be what the call writes (contiguous [M][N] of x's type
     and device), or a new tensor."""
@@ -312,7 +351,7 @@ def _call(fn_name: str, x: torch.Tensor, pw: PackedWeight, out=None, workspace=N
     y = _output(out, M, pw.N, x)
     nbytes = workspace_bytes(M, pw.N, pw.K, pw.group)
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = (workspace or _default_workspace(x.device, strm)).get(nbytes, strm)
+    ws = _scratch(workspace, x.device, strm, nbytes)
     ws_ptr = ws.data_ptr() if ws is not None else None
     ws_len = ws.numel() if ws is not None else 0
     fn_name = fn_name + "_fmt"
@@ -359,7 +398,7 @@ def linear_group(xs, pws, outs=None, workspace=None, stream=None):
                                                                            _fmt_code(pws[0].fmt), ctypes.byref(nb)))
     nbytes = nb.value
     strm = stream if stream is not None else torch.cuda.current_stream(xs[0].device)
-    ws = (workspace or _default_workspace(xs[0].device, strm)).get(nbytes, strm)
+    ws = _scratch(workspace, xs[0].device, strm, nbytes)
     zeros = arr([p.zeros_ptr() for p in pws]) if pws[0].zeros is not None else None
     _check("w4a16_linear_group_fmt", _lib.w4a16_linear_group_fmt(
         count, arr([x.data_ptr() for x in xs]), _dtype_code(xs[0]), arr([p.qweight.data_ptr() for p in pws]),
@@ -382,7 +421,7 @@ def linear_run(kernel: str, x, pw, out=None, workspace=None, stream=None):
     _check("w4a16_kernel_workspace_bytes", _lib.w4a16_kernel_workspace_bytes(code, M, pw.N, pw.K, pw.group,
                                                                              _fmt_code(pw.fmt), ctypes.byref(nb)))
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = (workspace or _default_workspace(x.device, strm)).get(nb.value, strm)
+    ws = _scratch(workspace, x.device, strm, nb.value)
     _check("w4a16_linear_run_fmt", _lib.w4a16_linear_run_fmt(
         code, x.data_ptr(), _dtype_code(x), pw.qweight.data_ptr(), pw.scales.data_ptr(), pw.zeros_ptr(),
         y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws.data_ptr() if ws is not None else None,
@@ -468,7 +507,7 @@ def linear_awq(x: torch.Tensor, act_mul: torch.Tensor, pw: PackedWeight, out=Non
     _check("w4a16_awq_workspace_bytes", _lib.w4a16_awq_workspace_bytes(M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt),
                                                                        _dtype_code(x), ctypes.byref(nb)))
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = (workspace or _default_workspace(x.device, strm)).get(nb.value, strm)
+    ws = _scratch(workspace, x.device, strm, nb.value)
     _check("w4a16_linear_awq", _lib.w4a16_linear_awq(
         x.data_ptr(), _dtype_code(x), act_mul.data_ptr(), pw.qweight.data_ptr(), pw.scales.data_ptr(),
         pw.zeros_ptr(), y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt),
