@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from ._lib import W4A16_BF16, W4A16_F16, _check, _lib, _scratch, _sz, _workspaces
+from ._lib import W4A16_BF16, W4A16_F16, _check, _lib, _queue, _sz, _workspaces
 
 _CODES = {torch.float16: W4A16_F16, torch.bfloat16: W4A16_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -208,19 +208,27 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
         os = _out_rows("out", out, shape, dtype, dev)
     nbytes = attention_workspace_bytes(batch, heads, kvh, dim, max_q_len, max_kv_len, window, sinks)
     raw = _raw_stream(dev)
-    buf = None   # held until the call is queued
-    if nbytes:
-        ws = _workspaces.get((dev, raw)) if workspace is None and not _capturing_here() else None
-        if ws is not None and ws.buf is not None and ws.buf.numel() >= nbytes and ws._alloc_stream.cuda_stream == raw:
-            buf = ws.buf   # (allocated on this stream: nothing to record)
-        else:
-            buf = _scratch(workspace, k_cache.device, torch.cuda.current_stream(dev), nbytes)
-    status = _attention_call(
-        q.data_ptr(), qs, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, page_stride, page_table.data_ptr(),
-        strides[0] if batch > 1 else columns, _index("kv_lens", kv_lens, torch.int32, (batch,), dev), starts,
-        tokens, batch, heads, kvh, dim, max_q_len, max_kv_len, dim ** -0.5 if scale is None else scale, window, sinks,
-        out.data_ptr(), os, None if lse is None else _index("lse", lse, torch.float32, (tokens, heads), dev),
-        None if buf is None else buf.data_ptr(), nbytes, raw)
+
+    def call(ws, ws_len):
+        return _attention_call(
+            q.data_ptr(), qs, code, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, page_stride, page_table.data_ptr(),
+            strides[0] if batch > 1 else columns, _index("kv_lens", kv_lens, torch.int32, (batch,), dev), starts,
+            tokens, batch, heads, kvh, dim, max_q_len, max_kv_len, dim ** -0.5 if scale is None else scale, window, sinks,
+            out.data_ptr(), os, None if lse is None else _index("lse", lse, torch.float32, (tokens, heads), dev), ws,
+            ws_len, raw)
+
+    status = None
+    if not nbytes:
+        status = call(None, 0)
+    elif workspace is None and not _capturing_here():
+        ws = _workspaces.get((dev, raw))
+        if ws is not None:
+            with ws.lock:
+                buf = ws.buf
+                if buf is not None and buf.numel() >= nbytes and ws._alloc_stream.cuda_stream == raw:
+                    status = call(buf.data_ptr(), nbytes)   # (allocated on this stream: nothing to record)
+    if status is None:
+        status = _queue(workspace, k_cache.device, torch.cuda.current_stream(dev), nbytes, call)
     if status:
         _check("w4a16_attention", status)
     return out

@@ -273,11 +273,16 @@ class Workspace:
     handed out under capture is never freed while the workspace lives, also
     where a later call needs a larger one. Graphs captured with one workspace
     must not replay at the same time.
+
+    Threads may share a workspace (and share a stream's own by default): a call
+    holds `lock` until all its launches are queued, so that none of another
+    thread's comes between two that pass partial results on.
     """
 
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else torch.device("cuda")
         self.buf = None
+        self.lock = threading.Lock()
         self._alloc_stream = None
         self._captured = False   # a graph holds self.buf's address
         self._outgrown = []      # buffers that graphs still hold
@@ -333,6 +338,16 @@ def _scratch(workspace, device, stream, nbytes: int):
     return _default_workspace(device, stream)._fit(nbytes, stream)
 
 
+def _queue(workspace, device, stream, nbytes: int, call):
+    """call(address, bytes) with its workspace, which is this thread's until
+    the call is queued."""
+    if nbytes == 0:
+        return call(None, 0)
+    with (workspace or _default_workspace(device, stream)).lock:
+        buf = _scratch(workspace, device, stream, nbytes)
+        return call(buf.data_ptr(), buf.numel())
+
+
 def _output(out, M: int, N: int, x: torch.Tensor) -> torch.Tensor:
     """`out`, checked to be what the call writes (contiguous [M][N] of x's type
     and device), or a new tensor."""
@@ -351,14 +366,11 @@ def _call(fn_name: str, x: torch.Tensor, pw: PackedWeight, out=None, workspace=N
     y = _output(out, M, pw.N, x)
     nbytes = workspace_bytes(M, pw.N, pw.K, pw.group)
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = _scratch(workspace, x.device, strm, nbytes)
-    ws_ptr = ws.data_ptr() if ws is not None else None
-    ws_len = ws.numel() if ws is not None else 0
     fn_name = fn_name + "_fmt"
     fn = getattr(_lib, fn_name)
-    _check(fn_name, fn(x.data_ptr(), _dtype_code(x), pw.qweight.data_ptr(), pw.scales.data_ptr(),
-                       pw.zeros_ptr(), y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws_ptr, ws_len,
-                       _stream_ptr(stream)))
+    _check(fn_name, _queue(workspace, x.device, strm, nbytes, lambda ws, ws_len: fn(
+        x.data_ptr(), _dtype_code(x), pw.qweight.data_ptr(), pw.scales.data_ptr(), pw.zeros_ptr(), y.data_ptr(), M,
+        pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws, ws_len, _stream_ptr(stream))))
     return y
 
 
@@ -398,13 +410,13 @@ def linear_group(xs, pws, outs=None, workspace=None, stream=None):
                                                                            _fmt_code(pws[0].fmt), ctypes.byref(nb)))
     nbytes = nb.value
     strm = stream if stream is not None else torch.cuda.current_stream(xs[0].device)
-    ws = _scratch(workspace, xs[0].device, strm, nbytes)
     zeros = arr([p.zeros_ptr() for p in pws]) if pws[0].zeros is not None else None
-    _check("w4a16_linear_group_fmt", _lib.w4a16_linear_group_fmt(
-        count, arr([x.data_ptr() for x in xs]), _dtype_code(xs[0]), arr([p.qweight.data_ptr() for p in pws]),
-        arr([p.scales.data_ptr() for p in pws]), zeros,
-        arr([y.data_ptr() for y in ys]), M, (ctypes.c_int64 * count)(*[p.N for p in pws]), K, group,
-        _fmt_code(pws[0].fmt), ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream_ptr(stream)))
+    _check("w4a16_linear_group_fmt", _queue(workspace, xs[0].device, strm, nbytes, lambda ws, ws_len: (
+        _lib.w4a16_linear_group_fmt(
+            count, arr([x.data_ptr() for x in xs]), _dtype_code(xs[0]), arr([p.qweight.data_ptr() for p in pws]),
+            arr([p.scales.data_ptr() for p in pws]), zeros,
+            arr([y.data_ptr() for y in ys]), M, (ctypes.c_int64 * count)(*[p.N for p in pws]), K, group,
+            _fmt_code(pws[0].fmt), ws, ws_len, _stream_ptr(stream)))))
     return ys
 
 
@@ -421,11 +433,10 @@ def linear_run(kernel: str, x, pw, out=None, workspace=None, stream=None):
     _check("w4a16_kernel_workspace_bytes", _lib.w4a16_kernel_workspace_bytes(code, M, pw.N, pw.K, pw.group,
                                                                              _fmt_code(pw.fmt), ctypes.byref(nb)))
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = _scratch(workspace, x.device, strm, nb.value)
-    _check("w4a16_linear_run_fmt", _lib.w4a16_linear_run_fmt(
-        code, x.data_ptr(), _dtype_code(x), pw.qweight.data_ptr(), pw.scales.data_ptr(), pw.zeros_ptr(),
-        y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws.data_ptr() if ws is not None else None,
-        ws.numel() if ws is not None else 0, _stream_ptr(stream)))
+    _check("w4a16_linear_run_fmt", _queue(workspace, x.device, strm, nb.value, lambda ws, ws_len: (
+        _lib.w4a16_linear_run_fmt(
+            code, x.data_ptr(), _dtype_code(x), pw.qweight.data_ptr(), pw.scales.data_ptr(), pw.zeros_ptr(),
+            y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws, ws_len, _stream_ptr(stream)))))
     return y
 
 
@@ -507,9 +518,7 @@ def linear_awq(x: torch.Tensor, act_mul: torch.Tensor, pw: PackedWeight, out=Non
     _check("w4a16_awq_workspace_bytes", _lib.w4a16_awq_workspace_bytes(M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt),
                                                                        _dtype_code(x), ctypes.byref(nb)))
     strm = stream if stream is not None else torch.cuda.current_stream(x.device)
-    ws = _scratch(workspace, x.device, strm, nb.value)
-    _check("w4a16_linear_awq", _lib.w4a16_linear_awq(
+    _check("w4a16_linear_awq", _queue(workspace, x.device, strm, nb.value, lambda ws, ws_len: _lib.w4a16_linear_awq(
         x.data_ptr(), _dtype_code(x), act_mul.data_ptr(), pw.qweight.data_ptr(), pw.scales.data_ptr(),
-        pw.zeros_ptr(), y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt),
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream_ptr(stream)))
+        pw.zeros_ptr(), y.data_ptr(), M, pw.N, pw.K, pw.group, _fmt_code(pw.fmt), ws, ws_len, _stream_ptr(stream))))
     return y
