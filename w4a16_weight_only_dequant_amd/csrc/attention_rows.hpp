@@ -42,6 +42,7 @@ constexpr int kRowsRT = 16;        // rows of a sequence and KV head at most
 constexpr int kRowsWaves = 4;
 constexpr int kRowsTK = 32;        // keys of a tile
 constexpr int kRowsUnit = 6;       // key tiles that the start and end of a row tile's part cost (4 us; a tile 0.6)
+constexpr float kRowsLift = 15.0f;   // fp16 weights are up to 2^15 (attn_against)
 constexpr int kRowsMaxSplits = 58;   // workgroups that share a row tile at most
 
 // Keys and values are read once: past the caches' retention (262 MB: 293 -> 264 us).
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(ALONE ? 64 : 64 * kRowsWaves, D == 64 ? 4 : D == 12
         for (int i = 1; i < 8; ++i) mx = fmaxf(mx, st[i >> 2][i & 3]);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float mn = fmaxf(m, mx * a.scale_log2);
+        const float mn = fmaxf(m, attn_against<BF>(mx, a.scale_log2, kRowsLift));
         const float ms = mn == -INFINITY ? 0.0f : mn;   // no key so far: every weight is exp2(-inf) = 0
         if (__any(mn > m)) {
             const float f = attn_exp2(m - ms);
@@ -314,8 +315,9 @@ __global__ __launch_bounds__(ALONE ? 64 : 64 * kRowsWaves, D == 64 ? 4 : D == 12
             w[i] = attn_exp2(fmaf(st[i >> 2][i & 3], a.scale_log2, -ms));
             l += w[i];
         }
-        // weights are rounded to the values' type for the product (l keeps them whole): a relative
-        // error of 2^-9 (bf16) or 2^-12 (f16) each, of random sign, below the output's own rounding
+        // weights are rounded to the values' type for the product (l keeps them whole): a relative error of 2^-8 (bf16)
+        // or 2^-11 (f16, down to the type's normal range) at most each, where they differ of random sign, as the
+        // output's own rounding
         const uint4 pf = make_uint4(attn_pack2<BF>(w[0], w[1]), attn_pack2<BF>(w[2], w[3]), attn_pack2<BF>(w[4], w[5]),
                                     attn_pack2<BF>(w[6], w[7]));
         if (poison) {
