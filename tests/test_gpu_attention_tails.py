@@ -32,7 +32,7 @@ def _few_large(news, below, n, dim, dtype, scale):
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("news", [1, 8])
+@pytest.mark.parametrize("news", [1, 8, 20])
 @pytest.mark.parametrize("below", [13.0, 16.25, 17.5])
 def test_many_small_weights_beside_a_few_large(dtype, dim, news, below):
     """exp(-13) .. exp(-17.5) of the largest weight, 131068 times, in sequences enough (of the same pages) that no
@@ -67,7 +67,7 @@ def test_many_small_weights_beside_a_few_large(dtype, dim, news, below):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("news", [1, 8])
+@pytest.mark.parametrize("news", [1, 8, 20])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_scores_of_millions(dtype, news, dim):
     """Scores whose steps in fp32 are larger than one: one key takes all, the weights stay in the type's range, and

@@ -23,8 +23,9 @@
 //   b64 reads of V (4 rows by 16 values, one operand quarter) touch every bank
 //   once.
 // * The running maximum is raised only when a row's new one exceeds it by more
-//   than 2^8 (in exp2 units 8): the weights then stay below 256, which the
-//   16-bit types hold as precisely, and the sums are rarely rescaled.
+//   than 2^8 (in exp2 units 8): the weights then stay below 256 (fp16: 2^15,
+//   carried 2^7 times larger), which the 16-bit types hold as precisely, and
+//   the sums are rarely rescaled.
 // * Step t of a wave is the product with V of tile t, and beside its matrix
 //   instructions the score maxima of tile t + 1; before it S of tile t + 1, and
 //   beside that the weights of tile t: vector work fills the issue slots that a
@@ -90,6 +91,7 @@ __device__ inline float attn_sum_halves(float x) {
 constexpr int kPromptTK = 32;   // keys of a tile
 constexpr int kPromptRows = 128;   // rows of a workgroup
 constexpr int kPromptMaxSplits = 64;   // workgroups that share a row tile's keys at most
+constexpr float kPromptLift = 7.0f;   // fp16 weights are up to 2^8, by the running maximum's lag, times 2^7 (attn_against)
 constexpr float kNone = -3e38f;   // a running maximum below every score: weights of hidden keys are exp2(-inf) = 0 beside it
 
 // What a lane keeps of its place, in LDS: read where a step needs it, before the step's barrier. (Kept in registers
@@ -141,7 +143,7 @@ struct AttnPrompt {
     // in order, and an MFMA keeps the matrix core for 32 clocks but the issue port for 4: the fences hold the mix in
     // which vector work fills the rest. Operands are read RING MFMAs ahead (an LDS read takes longer than an MFMA).
     // The weights (B operands of the second product) are rounded to the values' type; l keeps them whole (as in
-    // attention_rows.hpp).
+    // attention_rows.hpp; in fp16 those from 2^-21 of a row's largest on to 2^-11 of themselves).
     template <bool QK, bool W>
     __device__ __forceinline__ void front(uint32_t kb, attn_f16_t &nx, const attn_f16_t &cu, uint32_t vb, uint4 (&vf)[RING],
                                           uint4 (&p)[2]) {
@@ -228,7 +230,7 @@ struct AttnPrompt {
 
     // Raises the running maximum where a tile's, the larger of the halves' x, is more than 8 above it.
     __device__ __forceinline__ void maximum(float x) {
-        const float mn = attn_max_halves(x) * a.scale_log2;
+        const float mn = attn_against<BF>(attn_max_halves(x), a.scale_log2, kPromptLift);
         if (__any(mn > m + 8.0f)) {
             const float n = fmaxf(m, mn), f = attn_exp2(m - n);
             m = n;
