@@ -209,6 +209,43 @@ struct AttnPrompt {
         return __any((bad & 0x80008000u) != 0);
     }
 
+    // What infinities and NaN among the values of key tile `tile` add to the rows that see them, key by key: in the product they
+    // would reach the others too (a weight of 0 times NaN). A weight is positive: they add themselves. From memory once
+    // more, past the main loop, which has no registers for it.
+    __device__ __forceinline__ void apart(const AttnTiles<TK> &tiles, int tile, int b, int kvh) {
+        const int lane = attn_lane(), pos = mine->pos;
+#pragma unroll 1
+        for (int r = 0; r < TK; r += RPI) {
+            const int j = tiles.key(tile) + r + lane / CH;
+            int64_t at = 0;
+            int bad = 0;
+            if (j < tiles.hi) {
+                const int id = a.table[(int64_t)b * a.table_stride + (j >> a.page_log2)];
+                if ((unsigned)id < (unsigned)a.pages) {
+                    at = (int64_t)id * a.page_stride + (((int64_t)kvh << a.page_log2) + (j & ((1 << a.page_log2) - 1))) * D;
+                    bad = attn_nonfinite4<BF>(*reinterpret_cast<const attn_u4_t *>(a.vc + at + 8 * (lane % CH)));
+                }
+            }
+#pragma unroll 1
+            for (uint64_t left = __ballot(bad); left != 0;) {
+                const int first = __builtin_ctzll(left), k = first / CH;
+                left &= ~((CH == 64 ? ~0ull : (1ull << CH) - 1) << (k * CH));
+                const int64_t row = (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), first) << 32 |
+                                    (uint32_t)__builtin_amdgcn_readlane((int)at, first);
+                const int see = (int)attn_visible(tiles.key(tile) + r + k, pos, a.window, a.sinks);
+#pragma unroll
+                for (int q = 0; q < 4 * DB; ++q) {   // the lane's values 8 q + 4 half ..
+                    const attn_u2_t y = *reinterpret_cast<const attn_u2_t *>(a.vc + row + 8 * q + 4 * (lane >> 5));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint16_t z = (uint16_t)((e < 2 ? y.x : y.y) >> 16 * (e % 2));
+                        acc[q / 4][4 * (q % 4) + e] += see & attn_nonfinite<BF>(z) ? attn_to_f32<BF>(z) : 0.0f;
+                    }
+                }
+            }
+        }
+    }
+
     // Hides what the lane's row does not see: the tile's 32 keys as bits. gone: the 16-key groups that no row sees, as bits.
     __device__ __forceinline__ void hide(attn_f16_t &st, int j0, unsigned gone) {
         static_assert(TK == 32, "a tile's keys as bits of a word");
@@ -242,46 +279,13 @@ struct AttnPrompt {
     }
 };
 
-// One row's partial result (m, sum of weights, and the lane's D / 64 sums) over key tiles [t0, t1) with nothing but
-// what the row sees, key by key: for the row tiles whose values hold an infinity or a NaN in a tile that some rows see
-// in part only, where the matrix product would carry it to the others (a weight of 0 times NaN). A wave a row.
-template <int D, bool BF, int TK>
-__device__ void attn_row_by_key(const AttnArgs &a, const AttnTiles<TK> &tiles, int t0, int t1, int b, int kvh, int p,
-                                const uint16_t *q, float &m, float &l, float (&o)[D / 64]) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63;
-    float x[E];
-    m = -INFINITY;
-    l = 0.0f;
-    for (int e = 0; e < E; ++e) {
-        x[e] = attn_to_f32<BF>(q[lane * E + e]);
-        o[e] = 0.0f;
-    }
-    for (int t = t0; t < t1; ++t)
-        for (int j = tiles.key(t); j < min(tiles.key(t) + TK, tiles.hi); ++j) {
-            if (!attn_visible(j, p, a.window, a.sinks)) continue;
-            const int id = a.table[(int64_t)b * a.table_stride + (j >> a.page_log2)];
-            if ((unsigned)id >= (unsigned)a.pages) continue;
-            const int64_t at = (int64_t)id * a.page_stride +
-                               (((int64_t)kvh << a.page_log2) + (j & ((1 << a.page_log2) - 1))) * D + lane * E;
-            float s = 0.0f;
-            for (int e = 0; e < E; ++e) s += x[e] * attn_to_f32<BF>(a.kc[at + e]);
-            for (int f = 32; f > 0; f >>= 1) s += __shfl_xor(s, f);
-            s *= a.scale_log2;
-            const float n = fmaxf(m, s);
-            const float f = m == -INFINITY ? 0.0f : attn_exp2(m - n), w = attn_exp2(s - (n == -INFINITY ? 0.0f : n));
-            m = n;
-            l = l * f + w;
-            for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * attn_to_f32<BF>(a.vc[at + e]);
-        }
-}
-
 template <int D, bool BF, int NW, bool ONCE>
 __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_prompt_kernel(const AttnArgs a) {
     using P = AttnPrompt<D, BF, NW>;
     constexpr int TK = P::TK, CH = P::CH, BM = P::BM;
     __shared__ __align__(16) uint16_t lds[2][P::BUFS][TK * D];   // [K, V][buffer]
     __shared__ AttnLane lanes[64 * NW];
+    __shared__ int apart;   // 1: infinities or NaN in a tile that not every row sees whole, 2: in one that lacks a page
 
     // Workgroups go to the 8 XCDs in turn; a unit (sequence, KV head, split; splits slowest) stays on one, where its
     // row tiles find its keys in the L2, or, where units are few, its row tiles are dealt to a.slices of them, each with a
@@ -338,6 +342,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
         const int tok = sq.q0 + row / a.share, head = kvh * a.share + row % a.share;
         c.pos = pos0 + row / a.share;
         lanes[threadIdx.x] = c;
+        if (threadIdx.x == 0) apart = 0;
         s.mine = (const __attribute__((address_space(3))) AttnLane *)&lanes[threadIdx.x];
         const uint16_t *qp = a.q + (int64_t)tok * a.q_stride + (int64_t)head * D + 8 * half;
 #pragma unroll
@@ -406,24 +411,37 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
     // the same values: no barrier where nothing is cleared, as in the causal order's tiles of the row tile's own tokens.
     auto spoils = [&](int j0, unsigned g, uint32_t buffer, uint32_t vb) -> bool {
         if (j0 + TK > tiles.hi || max(j0, a.sinks) < min(tiles.lo, j0 + TK) || (g & 3) != 0) {
+            const uint32_t zero = attn_opaque(0);   // (no zeros in registers over the loop)
 #pragma unroll 1
-            for (int e = attn_opaque(threadIdx.x); e < TK * CH; e += 64 * NW) {
+            for (int e = 64 * s.wave + attn_opaque(attn_lane()); e < TK * CH; e += 64 * NW) {
                 const int r = e / CH, j = j0 + r;
                 if (j >= tiles.hi || (j < tiles.lo && j >= a.sinks) || ((g >> (r / 16)) & 1))
-                    *(__attribute__((address_space(3))) attn_u4_t *)(uintptr_t)(buffer + e * 16) = attn_u4_t{0, 0, 0, 0};
+                    *(__attribute__((address_space(3))) attn_u4_t *)(uintptr_t)(buffer + e * 16) = attn_u4_t{zero, zero, zero, zero};
             }
             __syncthreads();
         }
         return s.spoiled(vb);
+    };
+    // Such a tile: they are cleared for the product, and added to the rows that see them after the last tile.
+    auto clear = [&](unsigned g, uint32_t buffer) {
+        const int tid = 64 * s.wave + attn_opaque(attn_lane());
+        if (tid == 0) (&apart)[attn_opaque(0)] |= (g & 3) != 0 ? 3 : 1;
+        __syncthreads();
+#pragma unroll 1
+        for (int e = tid; e < TK * CH; e += 64 * NW) {
+            const auto p = (__attribute__((address_space(3))) attn_u4_t *)(uintptr_t)(buffer + e * 16);
+            const attn_u4_t x = *p;
+            *p = attn_u4_t{attn_finite<BF>(x.x), attn_finite<BF>(x.y), attn_finite<BF>(x.z), attn_finite<BF>(x.w)};
+        }
+        __syncthreads();
     };
 
     // Buffers go round: K of tile t + 1 and V of tile t are in LDS when step t starts, the next two of each on their
     // way. kb0: K of t + 1, then t + 2 and t + 3 (whose place K of t has left); vb0: V of t, then t + 1 and t + 2.
     uint32_t kb0 = lds0 + MAT, kb1 = lds0 + 2 * MAT, kb2 = lds0;
     uint32_t vb0 = lds0 + 3 * MAT, vb1 = lds0 + 4 * MAT, vb2 = lds0 + 5 * MAT;
-    // Step t: the weights of tile t beside S of tile t + 1, then the product of tile t beside the maxima of t + 1. False
-    // where the rows have to be summed key by key (uniform over the workgroup).
-    auto step = [&](int t, attn_f16_t &cu, attn_f16_t &nx) __attribute__((always_inline)) -> bool {
+    // Step t: the weights of tile t beside S of tile t + 1, then the product of tile t beside the maxima of t + 1.
+    auto step = [&](int t, attn_f16_t &cu, attn_f16_t &nx) __attribute__((always_inline)) {
         const uint32_t kv = s.mine->kv_at, ko = s.mine->ko, vo = s.mine->vo;
         // the loads of the step before last have landed: only the last step's may be under way
         if (t + 2 < t1)
@@ -438,7 +456,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
             find(t + 3, 3);
             load_k(ko, kb2);
         }
-        if (!plain(t, gone) && spoils(tiles.key(t), gone, vb0, vb0 + (kv >> 16))) return false;
+        if (!plain(t, gone) && spoils(tiles.key(t), gone, vb0, vb0 + (kv >> 16))) clear(gone, vb0);
         gone >>= 2;
         const uint32_t kb = kb0 + (kv & 0xFFFF), vb = vb0 + (kv >> 16);
         if (live) {
@@ -450,9 +468,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
         const uint32_t k = kb0, v = vb0;
         kb0 = kb1, kb1 = kb2, kb2 = k;
         vb0 = vb1, vb1 = vb2, vb2 = v;
-        return true;
     };
-    bool by_key = false;
     if (t0 < t1) {
         attn_f16_t sa, sb;
         uint4 vf[P::RING], p[2];
@@ -479,50 +495,34 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
         s.maximum(x);
         int t = t0;
         while (t + 1 < t1) {
-            by_key = !step(t, sa, sb);
+            step(t, sa, sb);
             ++t;
-            if (by_key) break;
             if (t + 1 >= t1) {
                 sa = sb;
                 break;
             }
-            by_key = !step(t, sb, sa);
+            step(t, sb, sa);
             ++t;
-            if (by_key) break;
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
-        if (!by_key) {   // the last tile
-            const uint32_t vb = vb0 + (s.mine->kv_at >> 16);
-            by_key = !plain(t, gone) && spoils(tiles.key(t), gone, vb0, vb);
-            if (!by_key) {
-                s.template front<false, true>(0, sa, sa, vb, vf, p);
-                s.back(sa, vb, vf, p);
-            }
+        // the last tile
+        const uint32_t vb = vb0 + (s.mine->kv_at >> 16);
+        if (!plain(t, gone) && spoils(tiles.key(t), gone, vb0, vb)) clear(gone, vb0);
+        s.template front<false, true>(0, sa, sa, vb, vf, p);
+        s.back(sa, vb, vf, p);
+        const int left = __builtin_amdgcn_readfirstlane(apart);
+        if (live && left != 0) {
+#pragma unroll 1
+            for (t = t0; t < t1; ++t)
+                if ((left & 2) != 0 || (unsigned)(t - plain0) >= (unsigned)plains) s.apart(tiles, t, b, kvh);
         }
     }
 
     const int lane = attn_opaque(attn_lane()), col = lane & 31, half = lane >> 5;
     const int pair_rt = (b * a.kv_heads + kvh) * a.row_tiles + rt;
     float *part = n_split > 1 ? a.part + ((int64_t)pair_rt * a.splits + split) * attn_part_floats(BM, D) : nullptr;
-    if (by_key) {
-        for (int lr = s.wave; lr < min(BM, rows - r0); lr += NW) {
-            const int tok = sq.q0 + (r0 + lr) / a.share, h = kvh * a.share + (r0 + lr) % a.share;
-            float m, l, o[D / 64];
-            attn_row_by_key<D, BF, TK>(a, tiles, t0, t1, b, kvh, pos0 + (r0 + lr) / a.share,
-                                       a.q + (int64_t)tok * a.q_stride + (int64_t)h * D, m, l, o);
-            const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-            if (n_split <= 1) {
-                for (int e = 0; e < D / 64; ++e)
-                    a.out[(int64_t)tok * a.out_stride + (int64_t)h * D + lane * (D / 64) + e] = attn_to_16<BF>(o[e] * inv);
-                if (lane == 0 && a.lse)
-                    a.lse[(int64_t)tok * a.heads + h] = m == -INFINITY ? -INFINITY : (m + __log2f(l)) * 0.693147180559945309f;
-            } else {
-                for (int e = 0; e < D / 64; ++e) part[lr * D + lane * (D / 64) + e] = o[e];
-                if (lane == 0) *reinterpret_cast<float2 *>(part + BM * D + 2 * lr) = make_float2(m, l);
-            }
-        }
-    } else {
+    {
         const float lt = attn_sum_halves(s.l0 + s.l1);
         const int mine = wr0 + col, row = min(mine, rows - 1);
         const int tok = sq.q0 + row / a.share, head = kvh * a.share + row % a.share;
