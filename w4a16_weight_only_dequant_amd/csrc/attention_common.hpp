@@ -70,6 +70,10 @@ __device__ __forceinline__ float attn_against(float x, float scale, float lift) 
     return fmaf(fabsf(m), 0x1.008p-24f, m);   // (-inf turns into NaN, which no maximum takes)
 }
 
+// ln of a row's sum: l weights of exp2(s - m). A row that sees nothing: l 0, -inf. One whose scores are NaN: l is NaN (m may
+// be any value, as no maximum takes a NaN).
+__device__ inline float attn_lse(float m, float l) { return (m + __log2f(l)) * 0.693147180559945309f; }
+
 // v, which the compiler no longer knows: what seldom-run code derives from it is computed there, not kept in registers
 // over the main loop (which has none to spare; a spill's reload would wait for the loads under way).
 __device__ __forceinline__ int attn_opaque(int v) {

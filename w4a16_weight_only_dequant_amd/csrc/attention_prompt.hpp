@@ -547,7 +547,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 ? 4 : D == 128 ? 3 : 1) void attn_
                             make_uint4((uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]);
                 }
             if (live && half == 0 && a.lse)
-                a.lse[(int64_t)tok * a.heads + head] = none ? -INFINITY : (s.m + __log2f(lt)) * 0.693147180559945309f;
+                a.lse[(int64_t)tok * a.heads + head] = attn_lse(s.m, lt);
         } else if (live) {
             const int lr = mine - r0;
 #pragma unroll
@@ -613,7 +613,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
             if (sub + 16 * k < n) weight[sub + 16 * k][row] = x[k].x * inv;
         if (sub == 0 && a.lse && r0 + row < rows) {
             const int tok = sq.q0 + (r0 + row) / a.share, h = kvh * a.share + (r0 + row) % a.share;
-            a.lse[(int64_t)tok * a.heads + h] = m == -INFINITY ? -INFINITY : (m + __log2f(l)) * 0.693147180559945309f;
+            a.lse[(int64_t)tok * a.heads + h] = attn_lse(m, l);
         }
     }
     __syncthreads();

@@ -437,14 +437,14 @@ __global__ __launch_bounds__(ALONE ? 64 : 64 * kRowsWaves, D == 64 ? 4 : D == 12
         float lr = 0.0f;
 #pragma unroll
         for (int v = 0; v < W; ++v)
-            lr += mr == -INFINITY ? 0.0f : ml[1][v][rr] * attn_exp2(ml[0][v][rr] - mr);
+            lr += ml[1][v][rr] * (mr == -INFINITY ? 0.0f : attn_exp2(ml[0][v][rr] - mr));
         if (whole) {
             const int tok = sq.q0 + rr / a.share, h = kvh * a.share + rr % a.share;
             const float inv = mr == -INFINITY ? 0.0f : 1.0f / lr;
             const uint2 v = make_uint2(attn_pack2<BF>(o.x * inv, o.y * inv), attn_pack2<BF>(o.z * inv, o.w * inv));
             *reinterpret_cast<uint2 *>(a.out + (int64_t)tok * a.out_stride + (int64_t)h * D + d) = v;
             if (d == 0 && a.lse)
-                a.lse[(int64_t)tok * a.heads + h] = mr == -INFINITY ? -INFINITY : (mr + __log2f(lr)) * 0.693147180559945309f;
+                a.lse[(int64_t)tok * a.heads + h] = attn_lse(mr, lr);
         } else {
             float *p = part + rr * D + d;
             attn_store2(p, o.x, o.y);
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(ALONE ? 64 : 64 * kRowsWaves, D == 64 ? 4 : D == 12
             const uint2 w = make_uint2(attn_pack2<BF>(o[k].x * inv, o[k].y * inv), attn_pack2<BF>(o[k].z * inv, o[k].w * inv));
             *reinterpret_cast<uint2 *>(a.out + (int64_t)tok * a.out_stride + (int64_t)h * D + d) = w;
             if (d == 0 && a.lse)
-                a.lse[(int64_t)tok * a.heads + h] = mr == -INFINITY ? -INFINITY : (mr + __log2f(lr)) * 0.693147180559945309f;
+                a.lse[(int64_t)tok * a.heads + h] = attn_lse(mr, lr);
         }
     };
     if (live * D / 4 <= 64 * W)
