@@ -27,8 +27,10 @@ def _on_device(fn, device, *args, **kw):
         return fn(*args, **kw)
 
 
-def _on_stream(fn, on, made, *args, **kw):
+def _on_stream(fn, on, made, device, *args, **kw):
     """fn on stream `on`: the copies and the result (if `made` there) belong to it too."""
+    if on.device != device:   # (the call would leave it for the caches' device)
+        raise ValueError(f"the stream is one of {on.device}, the caches are on {device}")
     caller = torch.cuda.current_stream(on.device)
     with torch.cuda.stream(on):
         got = fn(*args, **kw)
@@ -102,8 +104,8 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None, *,
     are the weights of a norm before it. Returns the queries, in q_out (which
     may be q) or a new tensor. Runs on `stream`, by default the current one."""
     if stream is not None:
-        return _on_stream(kv_append, stream, q_out is None, q, k, v, k_cache, v_cache, slots, positions, cos_sin, q_norm=q_norm,
-                          k_norm=k_norm, eps=eps, interleaved=interleaved, q_out=q_out)
+        return _on_stream(kv_append, stream, q_out is None, k_cache.device, q, k, v, k_cache, v_cache, slots, positions, cos_sin,
+                          q_norm=q_norm, k_norm=k_norm, eps=eps, interleaved=interleaved, q_out=q_out)
     dtype, code, dev, pages, kvh, page, dim, page_stride = _cache(k_cache, v_cache)
     if dev != _current_device():
         return _on_device(kv_append, dev, q, k, v, k_cache, v_cache, slots, positions, cos_sin, q_norm=q_norm,
@@ -174,7 +176,7 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
     where given, gets ln sum exp of each row's scores. workspace: a Workspace
     instead of the stream's own (under capture, of memory of the graph)."""
     if stream is not None:
-        return _on_stream(attention, stream, out is None, q, k_cache, v_cache, page_table, kv_lens, q_starts=q_starts,
+        return _on_stream(attention, stream, out is None, k_cache.device, q, k_cache, v_cache, page_table, kv_lens, q_starts=q_starts,
                           max_q_len=max_q_len, max_kv_len=max_kv_len, scale=scale, window=window, sinks=sinks, out=out,
                           lse=lse, workspace=workspace)
     dtype, code, dev, pages, kvh, page, dim, page_stride = _cache(k_cache, v_cache)
