@@ -938,8 +938,10 @@ w4a16_status w4a16_attention(const void *q, int64_t q_stride, int32_t dtype, con
     // out, lse and the workspace overlap no input and not each other
     const Range wr[] = {range_of(out, rows_span(tokens, out_stride, row)),
                         range_of(lse, lse ? (size_t)(tokens * heads) * 4 : 0), range_of(workspace, need)};
+    // (of the page table's last row only the columns that max_kv_len names: it may be a slice of a wider table)
+    const size_t table = (size_t)((batch - 1) * table_stride + ceil_div(max_kv_len, page_size)) * 4;
     const Range ins[] = {range_of(q, rows_span(tokens, q_stride, row)), range_of(k_cache, cache),
-                         range_of(v_cache, cache), range_of(page_table, (size_t)(batch * table_stride) * 4),
+                         range_of(v_cache, cache), range_of(page_table, table),
                          range_of(kv_lens, (size_t)batch * 4),
                          range_of(q_starts, q_starts ? (size_t)(batch + 1) * 4 : 0)};
     for (const Range &w : wr)
