@@ -453,7 +453,8 @@ w4a16_status w4a16_kv_append(const void *q, int64_t q_stride, const void *k, int
  * (0 .. max_kv_len), key j in page page_table[b * table_stride + j /
  * page_size]; its new tokens are rows [q_starts[b], q_starts[b+1]) of q, at
  * most max_q_len of them, the last of them at position kv_lens[b] - 1.
- * q_starts NULL: one token each (tokens = batch, max_q_len = 1).
+ * q_starts NULL: one token each (tokens = batch, max_q_len = 1). max_kv_len 0:
+ * no key anywhere, page_table is not read and may be NULL.
  *   visible(j, p) = j <= p and (window == 0 or j > p - window or j < sinks)
  *   s_j = scale * q . k_j;   lse = ln sum_visible exp(s_j)
  *   out = sum_visible exp(s_j - lse) v_j

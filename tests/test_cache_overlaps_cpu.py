@@ -36,3 +36,11 @@ def test_a_page_table_that_is_a_column_slice(attend):
     for bad in (dict(out=end - 16), dict(lse=end - 4), dict(out=table + 8), dict(lse=table)):
         assert _refused(attend(page_table=table, **bad)), bad
     assert _refused(attend(page_table=table, table_stride=19))
+
+
+def test_no_page_table_where_there_are_no_keys(attend):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("addresses here are not memory: with a device the call would go on to its launch")
+    assert not _refused(attend(page_table=None, max_kv_len=0, table_stride=0))
+    assert _refused(attend(page_table=None, max_kv_len=1))

@@ -24,3 +24,25 @@ def test_output_right_behind_a_column_slice(news):
     assert got is out
     c.check(out, lse)
     assert torch.equal(table, c.page_table) and bool((buf[:wide - columns] == -7).all())
+
+
+@pytest.mark.parametrize("news", [1, 30])
+def test_no_pages_at_all(news):
+    """Sequences without a key and a page table without a column: every row sees nothing."""
+    import w4a16_weight_only_dequant_amd as w4
+    c = Paged([5, 9], [news] * 2, 4, 2, 64, "f16", 16, seed=72)
+    lse = c.lse_buffer()
+    out = w4.attention(c.q_dev, c.k_cache, c.v_cache, c.page_table[:, :0], torch.zeros_like(c.kv_lens), q_starts=c.q_starts,
+                       max_q_len=news, lse=lse)
+    assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+    out = w4.attention(c.q_dev, c.k_cache, c.v_cache, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), torch.zeros_like(c.kv_lens),
+                       q_starts=c.q_starts, max_q_len=news)
+    assert bool((out == 0).all())
+    # a length that the page table has no room for is held to none, and reported
+    out = w4.attention(c.q_dev, c.k_cache, c.v_cache, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), c.kv_lens,
+                       q_starts=c.q_starts, max_q_len=news)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all())
+    with pytest.raises(w4.W4A16Error) as e:
+        w4.attention(c.q_dev, c.k_cache, c.v_cache, c.page_table, c.kv_lens, q_starts=c.q_starts, max_q_len=news)
+    assert e.value.status == 3

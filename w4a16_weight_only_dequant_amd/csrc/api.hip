@@ -924,7 +924,7 @@ w4a16_status w4a16_attention(const void *q, int64_t q_stride, int32_t dtype, con
     if (table_stride < ceil_div(max_kv_len, page_size) || table_stride > (1LL << 30)) return W4A16_ERR_INVALID_ARG;
     if (!q_starts && (tokens != batch || max_q_len != 1)) return W4A16_ERR_INVALID_ARG;
     if (tokens == 0 || batch == 0) return W4A16_OK;
-    if (!q || !k_cache || !v_cache || !page_table || !kv_lens || !out) return W4A16_ERR_INVALID_ARG;
+    if (!q || !k_cache || !v_cache || (!page_table && max_kv_len > 0) || !kv_lens || !out) return W4A16_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned(page_table, 4) ||
         !aligned(kv_lens, 4) || !aligned(q_starts, 4) || !aligned(lse, 4))
         return W4A16_ERR_INVALID_ARG;
