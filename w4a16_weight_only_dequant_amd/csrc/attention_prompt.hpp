@@ -65,7 +65,8 @@ __device__ inline int attn_swz_v(int r) {
 
 // 16 bytes a lane from global memory (`from` + `offset` bytes of the lane) straight into LDS at `to` + 16 lane; `from`
 // and `to` are uniform over the wave. Written as asm because the builtin makes the compiler wait for all such loads
-// before any LDS read that it cannot prove apart; no register is written, and the kernel itself waits (vmcnt(0))
+// before any LDS read that it cannot prove apart; no register but m0 is written (which is reserved: the compiler keeps
+// nothing in it, takes it in no clobber list, and uses it nowhere here), and the kernel itself waits (vmcnt)
 // before the barrier behind which the tile is read.
 // ONCE: read by this workgroup alone, past the caches' retention.
 template <bool ONCE>
