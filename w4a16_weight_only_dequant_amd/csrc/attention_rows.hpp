@@ -532,12 +532,14 @@ __global__ __launch_bounds__(ALONE ? 64 : 64 * kRowsWaves, D == 64 ? 4 : D == 12
                 a.lse[(int64_t)tok * a.heads + h] = attn_lse(mr, lr);
         }
     };
-    if (live * D / 4 <= 64 * W)
+    if (live * D / 4 <= 64 * W) {
         join(std::integral_constant<int, 1>{});
-    else if (live * D / 4 <= 128 * W)
-        join(std::integral_constant<int, 2>{});
-    else
-        join(std::integral_constant<int, 4>{});
+    } else if constexpr (D >= 128) {   // (16 rows of 64 values are one float4 a thread)
+        if (D == 128 || live * D / 4 <= 128 * W)
+            join(std::integral_constant<int, 2>{});
+        else
+            join(std::integral_constant<int, D / 64>{});
+    }
     attn_clear_flags(a, sp);
     }
     }
