@@ -46,3 +46,24 @@ def test_no_pages_at_all(news):
     with pytest.raises(w4.W4A16Error) as e:
         w4.attention(c.q_dev, c.k_cache, c.v_cache, c.page_table, c.kv_lens, q_starts=c.q_starts, max_q_len=news)
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("news", [1, 30])
+def test_strides_of_dimensions_of_one(news):
+    """A cache of one KV head kept as [pages][page_size][1][dim], a page table of one column kept as a row: the same memory,
+    with other strides where there is one of something."""
+    import w4a16_weight_only_dequant_amd as w4
+    c = Paged([14, 9, 16], [min(news, 9)] * 3, 4 if news == 1 else 8, 1, 64, "f16", 16, seed=73)
+    lse = c.lse_buffer()
+    kc, vc = (torch.empty(len(x), 16, 1, 64, dtype=x.dtype, device="cuda").transpose(1, 2).copy_(x) for x in (c.k_cache, c.v_cache))
+    table = c.page_table[:, 0].contiguous()
+    assert kc.stride(1) != c.k_cache.stride(1) and kc.data_ptr() != c.k_cache.data_ptr()
+    table = table.as_strided((3, 1), (1, 3))
+    for k, v in ((kc, vc), (kc, c.v_cache), (c.k_cache, vc)):
+        out = w4.attention(c.q_dev, k, v, table, c.kv_lens, q_starts=c.q_starts, max_q_len=max(c.news), lse=lse)
+        c.check(out, lse)
+    # appending through such a view writes the cache itself
+    new = torch.randn(2, 1, 64, device="cuda").to(torch.float16)
+    w4.kv_append(None, new, new, kc, vc, torch.tensor([15, 5], device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(kc[0, 0, [15, 5]], new[:, 0]) and torch.equal(vc[0, 0, [15, 5]], new[:, 0])

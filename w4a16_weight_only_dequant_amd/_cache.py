@@ -78,10 +78,12 @@ def _cache(k_cache, v_cache):
         raise ValueError("v_cache must have k_cache's shape, type and device")
     pages, kvh, page, dim = shape
     s0, s1, s2, s3 = k_cache.stride()
-    strides = v_cache.stride()
-    if s1 != page * dim or s2 != dim or s3 != 1 or strides[1:] != (s1, dim, 1) or (strides[0] != s0 and pages > 1):
+    t0, t1, t2, t3 = v_cache.stride()
+    row = page * dim
+    # (a dimension of one may have any stride)
+    if s2 != dim or t2 != dim or s3 != 1 or t3 != 1 or (kvh > 1 and (s1 != row or t1 != row)) or (pages > 1 and s0 != t0):
         raise ValueError("the caches' pages must be contiguous [kv_heads][page_size][dim], equally far apart")
-    return dtype, code, dev, pages, kvh, page, dim, s0 if pages > 1 else kvh * s1
+    return dtype, code, dev, pages, kvh, page, dim, s0 if pages > 1 else kvh * row
 
 
 def _index(name, t, dtype, shape, dev):
@@ -187,9 +189,11 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
     q, qs, shape = _rows("q", q, dtype, dev, dim)
     tokens, heads, _ = shape
     strides = page_table.stride()
-    if len(strides) != 2 or page_table.dtype != torch.int32 or page_table.get_device() != dev or strides[1] != 1:
+    if len(strides) != 2 or page_table.dtype != torch.int32 or page_table.get_device() != dev:
         raise ValueError(f"page_table must be an int32 tensor [batch][pages of a sequence] on cuda:{dev}")
     batch, columns = page_table.shape
+    if strides[1] != 1 and columns > 1:
+        raise ValueError("page_table must be a tensor of contiguous rows")
     if max_kv_len is None:
         max_kv_len = columns * page
     elif max_kv_len > columns * page:
