@@ -41,8 +41,8 @@ def _on_stream(fn, on, made, device, *args, **kw):
 
 def _rows(name, t, dtype, dev, dim):
     """t as [tokens][heads][dim] rows the kernels take: heads contiguous, the
-    token stride a multiple of 8 (a copy where they are not). Returns it with
-    that stride and its shape."""
+    token stride a multiple of 8, the first on 16 bytes (a copy where they are
+    not). Returns it with that stride and its shape."""
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or t.dtype != dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {dtype} tensor [tokens][heads][{dim}] on cuda:{dev}")
@@ -50,8 +50,8 @@ def _rows(name, t, dtype, dev, dim):
     row = shape[1] * dim
     if shape[0] <= 1:
         s0 = row
-    if s2 != 1 or s0 % 8 or s0 < row or (s1 != dim and shape[1] != 1):
-        return t.contiguous(), row, shape
+    if s2 != 1 or s0 % 8 or s0 < row or (s1 != dim and shape[1] != 1) or t.data_ptr() % 16:
+        return t.clone(memory_format=torch.contiguous_format), row, shape
     return t, s0, shape
 
 
@@ -63,8 +63,8 @@ def _out_rows(name, t, shape, dtype, dev):
     row = shape[1] * shape[2]
     if shape[0] <= 1:
         s0 = row
-    if s2 != 1 or s0 % 8 or s0 < row or (s1 != shape[2] and shape[1] != 1):
-        raise ValueError(f"{name}'s heads must be contiguous and its token stride a multiple of 8")
+    if s2 != 1 or s0 % 8 or s0 < row or (s1 != shape[2] and shape[1] != 1) or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s heads must be contiguous, its token stride a multiple of 8 and its start on 16 bytes")
     return s0
 
 
