@@ -463,13 +463,17 @@ w4a16_status w4a16_kv_append(const void *q, int64_t q_stride, const void *k, int
  * and lse = -inf. What a row does not see never reaches it, whatever it holds
  * (infinities and NaN included). Running maximum, sums and outputs are fp32;
  * the softmax weights are rounded to the cache's type for the second product
- * and out once to its type. lse (fp32 [tokens][heads]) may be NULL. Rows of q
+ * (fp16: scaled up first, so that small ones keep their value) and out once to
+ * its type. A row with a score of NaN gets NaN and lse NaN. lse (fp32 [tokens][heads]) may be NULL. Rows of q
  * that belong to no sequence are not written.
  *
  * Up to 16 rows (max_q_len * heads / kv_heads) stream the cache through
  * registers, all sequences' keys divided evenly over the compute units; more
  * take tiles of keys through LDS, 128 rows a workgroup, and a second launch
- * that joins them where keys are divided. The same call gives the same bits every time;
+ * that joins them where keys are divided, by max_q_len and max_kv_len alone: a
+ * sequence of few tokens over far more keys than the others belongs in a call of
+ * its own (one token over 131072 keys beside a prompt of 512: 2.9 ms, apart 0.11).
+ * The same call gives the same bits every time;
  * where a sequence's keys are divided depends on the other lengths too, so
  * its last bits may differ in another batch.
  * Workspace (16-byte aligned, no initialisation, as w4a16_workspace_bytes):

@@ -104,7 +104,8 @@ def kv_append(q, k, v, k_cache, v_cache, slots, positions=None, cos_sin=None, *,
     int32 [tokens] and cos_sin float32 [max_positions][rot_dim] (cosines, then
     sines) rotate the first rot_dim values of q and k; q_norm and k_norm [dim]
     are the weights of a norm before it. Returns the queries, in q_out (which
-    may be q) or a new tensor. Runs on `stream`, by default the current one."""
+    may be q) or a new tensor; a token whose slot or position is out of range is
+    left out, and the next call reports it. Runs on `stream`, by default the current one."""
     if stream is not None:
         return _on_stream(kv_append, stream, q_out is None, k_cache.device, q, k, v, k_cache, v_cache, slots, positions, cos_sin,
                           q_norm=q_norm, k_norm=k_norm, eps=eps, interleaved=interleaved, q_out=q_out)
@@ -176,7 +177,10 @@ def attention(q, k_cache, v_cache, page_table, kv_lens, *, q_starts=None, max_q_
     keys (itself among them) and the first `sinks` of its sequence; 0: all.
     Returns the output, in `out` or a new tensor; lse float32 [tokens][heads],
     where given, gets ln sum exp of each row's scores. workspace: a Workspace
-    instead of the stream's own (under capture, of memory of the graph)."""
+    instead of the stream's own (under capture, of memory of the graph).
+    Rows of q that belong to no sequence are not written: a new tensor holds
+    anything there. Single tokens over long caches belong in a call of their
+    own, not beside prompts."""
     if stream is not None:
         return _on_stream(attention, stream, out is None, k_cache.device, q, k_cache, v_cache, page_table, kv_lens, q_starts=q_starts,
                           max_q_len=max_q_len, max_kv_len=max_kv_len, scale=scale, window=window, sinks=sinks, out=out,

@@ -59,7 +59,7 @@ __device__ inline float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // What a tile's scores, `x` the largest, are held against (exp2 units): weights are exp2(s * scale - m). fp16 holds
 // nothing below 2^-25, and many small weights are much: 131068 keys exp(-17.5) below four others are 0.08 % of the sum,
-// and were none of the product. So fp16 weights are carried 2^lift times larger, m smaller, to the top of the type's range;
+// and would be none of the product. So fp16 weights are carried 2^lift times larger, m smaller, to the top of the type's range;
 // sums are carried alike, and lse = m + log2(l) holds as it stands. m is rounded up by a step, so that a weight of scores
 // whose steps are larger than one cannot pass the range (the products s * scale are not rounded beside m). Weights 2^-29
 // of a part's largest (few rows, many rows 2^-21) keep their relative precision, smaller ones an absolute 2^-40 (2^-32).

@@ -30,11 +30,13 @@
 //   instructions the score maxima of tile t + 1; before it S of tile t + 1, and
 //   beside that the weights of tile t: vector work fills the issue slots that a
 //   matrix instruction leaves (front, back).
-// Measured: 8192 tokens, a window of 2048, 64 heads on 8 of 128, bf16: 505 us,
-// 954 TFLOP/s; ragged prompts of up to 1900 tokens behind 1500 keys, f16: 677 us,
-// 915; a library product of 8192 x 8192 x 8192 reaches 1313 (bf16) and 1250 (f16).
+// Measured: 8192 tokens, a window of 2048, 64 heads on 8 of 128, bf16: 500 us,
+// 963 TFLOP/s; ragged prompts of up to 1900 tokens behind 1500 keys, f16: 673 us,
+// 921; a library product of 8192 x 8192 x 8192 reaches 1313 (bf16) and 1250 (f16).
 // The matrix cores are busy 51 % of the time at the 1.8 GHz that the power limit
-// leaves, the vector units 57 %, LDS 29 %.
+// leaves, the vector units 59 %, LDS 30 %. Dim 64 fills the vector units first (62 %
+// beside 32 %: 4096 tokens of 40 heads 118 us, 728 TFLOP/s); dim 256 has one wave a
+// SIMD, whose waits nothing fills (25 % and 21 %: 16 heads on 4 213 us, 645).
 #pragma once
 
 #include "attention_common.hpp"
