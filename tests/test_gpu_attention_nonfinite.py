@@ -103,8 +103,8 @@ def test_a_missing_page_beside_them(w4, dim):
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("what", ["one", "all"])
 def test_their_cost_is_bounded(w4, dim, what):
-    """Row tiles whose own tokens' values hold one NaN, or hundreds of infinities, behind 6000 keys: a few times the call
-    without them at most."""
+    """Row tiles whose own tokens' values hold one NaN, or hundreds of infinities, behind 6000 keys: some
+    times the call without them (1.05 and 7 at most), not hundreds as where all keys of a row tile are gone through."""
     c = Paged([6020], [20], 8, 2, dim, "bf16", 64, seed=53)
     batch = 260                      # of the same pages: enough row tiles that no one's keys are divided
     q, table = c.q_dev.repeat(batch, 1, 1), c.page_table.repeat(batch, 1)
@@ -125,4 +125,4 @@ def test_their_cost_is_bounded(w4, dim, what):
            else [(0, 6010, h, 5, math.nan) for h in range(2)])
     spoilt = timed()
     print(f"{clean * 1e3:.0f} us, {spoilt * 1e3:.0f} us with them")
-    assert spoilt < 10 * clean
+    assert spoilt < 30 * clean
